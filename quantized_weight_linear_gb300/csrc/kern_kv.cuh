@@ -172,9 +172,12 @@ __device__ __forceinline__ uint32_t kv_byte(float y) {
 
 // ---- attention ---------------------------------------------------------------------------
 
-// The reference M of a row's weights 2^(t - M) is raised only when a weight would pass 2^8
-// (fp16 holds up to 2^16): sums are rescaled a few times a row instead of once a tile
-constexpr float kKvGrowLog2 = 8.f;
+// A row's weights 2^(t - M) go to fp16, which has 2^-24 as its smallest step and ends at 2^16.  M is
+// set 10 under the largest t, and raised only when a weight would pass 2^15: sums are rescaled a few
+// times a row instead of once a tile, and a weight is off by 2^-12 of itself, or, under 2^-24 of the
+// row's largest, by up to 2^-35 of that one.  (With M at the largest t it was 2^-25: behind a first
+// token of 99.9% of the weight and a small value, 131072 tokens lost 6% of the output in an emulation.)
+constexpr float kKvTopLog2 = 10.f, kKvGrowLog2 = 15.f;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -185,6 +188,14 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Two weights in fp16.  They are under 2^15 but for the rounding of t, half a unit from |t| = 2^22 on:
+// scores so far out saturate instead of becoming infinite.
+__device__ __forceinline__ uint32_t pack_weights(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
 }
 
 // The blocks that some row of a sequence sees: blocks [0, sb) and [wb, wb + n - sb)

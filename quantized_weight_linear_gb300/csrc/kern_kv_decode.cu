@@ -5,8 +5,8 @@
 // bare codes, exact in fp16 (m16n8k16 MMAs, fp32 accumulators), and both scales ride on the
 // exponent: with t_ij = (q_i . ck_j) (scale log2(e) ks_b) + log2(vs_b),
 //   p_ij = 2^(t_ij - M_i),  O_i = sum p_ij cv_j / L_i,  L_i = sum p_ij / vs_b,
-// one FMA and one exponential an element.  p <= 2^8 goes to fp16 (11 bits: the error of a
-// weight is 2^-12 of it); M, L and O stay in fp32.  Queries are scaled by a power of two per row
+// one FMA and one exponential an element.  p < 2^15 goes to fp16 (11 bits; kern_kv.cuh says where M is
+// and what that does to small weights); M, L and O stay in fp32.  Queries are scaled by a power of two per row
 // so that the row's largest element is in [1, 2): bf16 to fp16 is then exact but for elements
 // under 2^-14 of the largest, and cannot overflow.
 //
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::kThreads, 1) kv_decode_kernel(c
               float v = top[nt][h];
 #pragma unroll
               for (int s = 4; s < 32; s <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, s));
-              v = fmaxf(v, m[nt][h]);
+              v = fmaxf(v - kKvTopLog2, m[nt][h]);
               const float f = m[nt][h] == -INFINITY ? 0.f : ex2(m[nt][h] - v);
               m[nt][h] = v;
               l[nt][h] *= f;
@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::kThreads, 1) kv_decode_kernel(c
               const float p0 = ex2(fmaf(x[nt][i][2 * e], kb[nt][0], off0)), p1 = ex2(fmaf(x[nt][i][2 * e + 1], kb[nt][1], off1));
               s0 += p0;
               s1 += p1;
-              pb[nt][i][e] = transpose8(pack_f16x2(p0, p1));
+              pb[nt][i][e] = transpose8(pack_weights(p0, p1));
             }
           l[nt][0] = fmaf(s0, biv, l[nt][0]);
           l[nt][1] = fmaf(s1, biv, l[nt][1]);

@@ -833,7 +833,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const PreArgs p
               top = fmaxf(top, fmaf(v, k.x, k.y));
             }
             if (__any_sync(0xffffffffu, top > m + kKvGrowLog2)) {
-              const float mn = fmaxf(m, top);
+              const float mn = fmaxf(m, top - kKvTopLog2);
               const float f = m == -INFINITY ? 0.f : ex2(m - mn);
               m = mn;
               l *= f;
@@ -868,7 +868,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const PreArgs p
                     p0 = ex2(p0);
                     p1 = ex2(p1);
                     sum2 = add2(sum2, pack2(p0, p1));
-                    w[8 * b + e] = pack_f16x2(p0, p1);
+                    w[8 * b + e] = pack_weights(p0, p1);
                   }
                   float s0, s1;
                   unpack2(sum2, s0, s1);
@@ -913,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const PreArgs p
               }
             }
             if (__any_sync(0xffffffffu, top > m + kKvGrowLog2)) {
-              const float mn = fmaxf(m, top);
+              const float mn = fmaxf(m, top - kKvTopLog2);
               const float f = m == -INFINITY ? 0.f : ex2(m - mn);
               m = mn;
               l *= f;
@@ -946,7 +946,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const PreArgs p
                   p0 = ex2(p0);
                   p1 = ex2(p1);
                   sum2 = add2(sum2, pack2(p0, p1));
-                  w[8 * b + e] = pack_f16x2(p0, p1);
+                  w[8 * b + e] = pack_weights(p0, p1);
                 }
                 float s0, s1;
                 unpack2(sum2, s0, s1);

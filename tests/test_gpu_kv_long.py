@@ -1,0 +1,157 @@
+"""Attention over the 8-bit cache on long contexts and big batches, against float64 in plain PyTorch
+on the GPU (the numpy oracle of the other tests is too slow for these sizes).
+
+Bars, derived before any run, term by term as in the tests of short contexts, but with the weights' range:
+a row's fp16 weights are held with their largest at 2^10 or above, so a small one is off by at most 2^-25 of
+2^-10 of the largest, which moves an output by up to 2^-35 max(p vs) sum|cv| (p: weights, vs, cv: scales and
+codes of the values).  With a factor of 16 of room for that term and 2 for the others:
+|o - o_ref| <= 2^-8 |o_ref| + (2^-10 + 2^-14 (1 + mag)) sum p|v| + 2^-31 max(p vs) sum|cv|,
+|lse - ref| <= 2^-16 (1 + mag), mag = the row's largest scale * sum |q||k|.
+"""
+import numpy as np
+import pytest
+
+from oracle import kv as okv
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+class Long:
+    """One long sequence of T tokens in the cache (pages in a shuffled order), which the sequences of a
+    batch share: sequence b is its first kv_lens[b] tokens."""
+
+    def __init__(self, qlin, code, D, page, H, T, seed=0, keys=1.0, values=1.0, mean=0.0):
+        self.qlin, self.code, self.D, self.page, self.H, self.T = qlin, code, D, page, H, T
+        g = self.g = torch.Generator(device="cuda").manual_seed(seed)
+        n = -(-T // page)
+        self.order = torch.randperm(n + 2, generator=g, device="cuda")[:n].to(torch.int32)
+        k = torch.randn(T, H, D, generator=g, device="cuda") * keys
+        v = torch.randn(T, H, D, generator=g, device="cuda") * values + mean
+        self.codes = torch.randint(0, 256, (n + 2, H, 2, page * D), generator=g, device="cuda", dtype=torch.uint8)
+        self.scales = torch.full((n + 2, H, page // 16, 2), float("nan"), device="cuda")
+        self.cache = qlin.KVCache(self.codes, self.scales, code)
+        self.store(k, v)
+
+    def store(self, k, v):
+        """Quantizes k, v [T, H, D] block by block, in plain PyTorch."""
+        T, page, top = self.T, self.page, float(okv.QMAX[self.code])
+        nb = page // 16
+        for which, x in ((0, k), (1, v)):
+            pad = torch.zeros((self.order.numel() * page, self.H, self.D), device="cuda")
+            pad[:T] = x
+            b = pad.view(-1, nb, 16, self.H, self.D).permute(0, 3, 1, 2, 4)  # page, head, block, token, element
+            s = (b.abs().amax((3, 4)) / top).clamp_min(2.0 ** -60)
+            y = b / s[..., None, None]
+            if self.code == "int8":
+                byte = (y.round().clamp(-127, 127) + 128).to(torch.uint8)
+            else:
+                byte = y.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+            if which:
+                byte = byte.transpose(3, 4)  # a block's tokens innermost
+            at = self.order.long()
+            self.codes[at, :, which] = byte.reshape(len(at), self.H, page * self.D)
+            self.scales[at, :, :, which] = s
+
+    def batch(self, q_lens, kv_lens):
+        cols = max(-(-max(kv_lens) // self.page), 1)
+        pages = self.order[:cols].expand(len(kv_lens), cols).contiguous()
+        return self.qlin.KVBatch(i32(np.concatenate([[0], np.cumsum(q_lens)])), i32(kv_lens), pages, int(sum(q_lens)),
+                                 max(q_lens), max(kv_lens))
+
+    def held(self):
+        """Codes and scales of the keys and values, [H, T, D] and [H, T, 1], float64."""
+        nb, at, out = self.page // 16, self.order.long(), []
+        for which in (0, 1):
+            c = self.codes[at, :, which]
+            c = c.double() - 128 if self.code == "int8" else c.view(torch.float8_e4m3fn).double()
+            shape = (-1, self.H, nb, self.D, 16) if which else (-1, self.H, nb, 16, self.D)
+            c = c.reshape(shape)
+            if which:
+                c = c.transpose(3, 4)
+            c = c.permute(1, 0, 2, 3, 4).reshape(self.H, -1, self.D)[:, :self.T]
+            s = self.scales[at][..., which].double().permute(1, 0, 2)[..., None].expand(-1, -1, -1, 16)
+            out += [c, s.reshape(self.H, -1, 1)[:, :self.T]]
+        return out
+
+    def check(self, q_lens, kv_lens, q, o, lse, scale, rows=None, window=0, sinks=0):
+        """Compares the given rows (token, query head), all by default."""
+        kc, ks, vc, vs = self.held()
+        hq = q.shape[1]
+        group = hq // self.H
+        starts = np.concatenate([[0], np.cumsum(q_lens)])
+        worst = 0.0
+        for b, (n, kv) in enumerate(zip(q_lens, kv_lens)):
+            tokens = [t for t in range(n) if rows is None or (b, t) in rows]
+            if not tokens:
+                continue
+            t = torch.tensor(tokens, device="cuda")
+            pos = kv - n + t
+            j = torch.arange(kv, device="cuda")
+            seen = j <= pos[:, None]
+            if window:
+                seen &= (j > pos[:, None] - window) | (j < sinks)
+            for h in range(self.H):
+                x = q[starts[b] + t, h * group:(h + 1) * group].double()  # [t, g, D]
+                K, V = kc[h, :kv] * ks[h, :kv], vc[h, :kv] * vs[h, :kv]
+                w = (x @ K.T * scale).masked_fill(~seen[:, None], -torch.inf)
+                m = w.amax(-1, keepdim=True)
+                none = torch.isneginf(m)
+                p = torch.exp(w - torch.where(none, torch.zeros_like(m), m))
+                total = p.sum(-1, keepdim=True)
+                p = torch.where(none, torch.zeros_like(p), p / torch.where(none, torch.ones_like(total), total))
+                ref = p @ V
+                mag = ((x.abs() @ K.abs().T * scale) * seen[:, None]).amax(-1, keepdim=True)
+                codes = seen.double() @ vc[h, :kv].abs()
+                tol = 2.0 ** -8 * ref.abs() + (2.0 ** -10 + 2.0 ** -14 * (1 + mag)) * (p @ V.abs()) + \
+                    2.0 ** -31 * (p * vs[h, :kv, 0]).amax(-1, keepdim=True) * codes[:, None]
+                got = o[starts[b] + t, h * group:(h + 1) * group].double()
+                assert bool(torch.isfinite(got).all())
+                worst = max(worst, float(((got - ref).abs() / tol.clamp_min(1e-300)).max()))
+                l = lse[starts[b] + t, h * group:(h + 1) * group, None].double()
+                want = m + torch.log(total)
+                assert bool((torch.isneginf(l) == none).all())
+                assert bool((((l - want).abs() <= 2.0 ** -16 * (1 + mag)) | none).all())
+        assert worst <= 1, f"worst {worst}"
+
+
+def bf(x):
+    return x.to(torch.bfloat16)
+
+
+def some_rows(q_lens, n, seed):
+    """n sequences, of each its first and last token and one between."""
+    rng = np.random.default_rng(seed)
+    live = [b for b, q in enumerate(q_lens) if q]
+    pick = rng.choice(live, min(n, len(live)), replace=False)
+    return {(int(b), int(t)) for b in pick for t in (0, q_lens[b] - 1, rng.integers(q_lens[b]))}
+
+
+@pytest.mark.parametrize("code,D", [("int8", 64), ("e4m3", 128)])
+@pytest.mark.parametrize("seqs,q_len,group", [(480, 1, 4), (480, 2, 8), (76, 16, 4), (38, 96, 4)])
+def test_dominant_first_token(qlin, code, D, seqs, q_len, group):
+    """A first token with 99.9% of the weight and a small value, before 32768 tokens whose values have a
+    common mean: what they add up to is a tenth of the output.  So many sequences that a warp (a CTA, for
+    prompts) has whole items, whose weights are held against the one large one all along."""
+    T, H = 32768, 2
+    su = Long(qlin, code, D, 64, H, T, seed=seqs, keys=0.02, mean=1.0, values=0.3)
+    direction = torch.randn(H, D, generator=su.g, device="cuda")
+    k = torch.randn(T, H, D, generator=su.g, device="cuda") * 0.02
+    v = torch.randn(T, H, D, generator=su.g, device="cuda") * 0.3 + 1.0
+    q = direction.repeat_interleave(group, 0) + 0.02 * torch.randn(seqs * q_len, H * group, D, generator=su.g, device="cuda")
+    scale = D ** -0.5
+    k[0] = direction * (np.log(999.0 * T) / (scale * (direction ** 2).sum(-1, keepdim=True)))
+    v[0] = 0.01 * torch.randn(H, D, generator=su.g, device="cuda")
+    su.store(k, v)
+    q_lens, kv_lens = [q_len] * seqs, [T - b % 16 for b in range(seqs)]
+    q = bf(q)
+    o, lse = su.cache.attend(su.batch(q_lens, kv_lens), q, return_lse=True)
+    assert su.cache.poll_status() == 0
+    su.check(q_lens, kv_lens, q, o, lse, scale, some_rows(q_lens, 6, seqs))
