@@ -275,6 +275,8 @@ qlin_status qlin_poll_status(qlin_handle h, qlin_stream stream);
  * which are the LAST ones of its kv_len[b] tokens: the i-th sits at position
  * kv_len[b] - (q_start[b + 1] - q_start[b]) + i.  Tokens at a negative position are padding
  * (an unused slot of the batch has kv_len 0): they store nothing, see nothing and get zeros.
+ * A step may have rows that no sequence has (total_q above q_start[n_seqs]): qlin_kv_attend and
+ * qlin_kv_read leave their outputs as they are, qlin_kv_append gives their queries zeros.
  * pages[b * pages_stride + j] is the page of tokens j * page_tokens and up.  The arrays are
  * device memory and read by the kernels, so a captured graph follows their contents.
  *

@@ -145,7 +145,8 @@ qlin_status qlin_kv_attend(const qlin_kv_cache* c, const qlin_kv_batch* b, const
   const int sms = attend_sms();
   const bool uniform = a.batch.n_seqs == 1 || (int64_t)a.batch.max_q * a.batch.n_seqs == a.batch.total_q;
   const int64_t most = (int64_t)std::min(a.batch.max_q, a.batch.total_q) * a.group;
-  const int64_t least = a.batch.n_seqs == 1 ? (int64_t)a.batch.total_q * a.group : uniform ? most : 1;
+  // (a step may have rows that no sequence has: total_q says nothing of a sequence's rows)
+  const int64_t least = uniform ? most : 1;
   a.min_rows = 1;
   a.max_rows = most <= kKvDecodeRows ? INT32_MAX : kKvDecodeRows;
   int e = 0;

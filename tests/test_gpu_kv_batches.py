@@ -1,0 +1,37 @@
+"""Batches of the 8-bit cache calls that hold less, or other, than their sizes let one expect: rows that no
+sequence has, and index arrays that make no sense (reported, and never followed).  Bars as in test_gpu_kv."""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+from test_gpu_kv import Setup, bf, check_attend, i32  # noqa: E402
+
+
+@pytest.mark.parametrize("group", [1, 4, 16, 20])
+@pytest.mark.parametrize("q_len,max_q,rows", [(1, 1, 8), (1, 1, 40), (3, 4, 9), (5, 5, 300), (0, 1, 8), (40, 60, 64)])
+def test_one_sequence_in_a_longer_step(qlin, group, q_len, max_q, rows):
+    """One sequence whose step has rows behind it that are not in use: its rows, on both sides of the limit
+    between the kernels, are right, and the others are left alone."""
+    H, D = 2, 64
+    su = Setup(qlin, "int8", D, 32, H, [q_len], [150], seed=group)
+    q = su.rows(H * group, T=rows)
+    b = qlin.KVBatch(i32([0, q_len]), i32([150]), i32(su.pages), rows, max_q, 150)
+    o = torch.full((rows, H * group, D), 77.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((rows, H * group), 77.0, device="cuda")
+    su.cache.attend(b, bf(q), out=o, lse=lse)
+    su.ok()
+    check_attend(su, q[:q_len], H * group, o[:q_len], lse[:q_len], D ** -0.5)
+    assert bool((o[q_len:] == 77).all()) and bool((lse[q_len:] == 77).all())
+
+
+@pytest.mark.parametrize("group", [1, 4, 20])
+@pytest.mark.parametrize("n,max_q,rows", [(8, 1, 8), (30, 4, 30), (300, 5, 300)])
+def test_one_sequence_with_more_tokens_than_said(qlin, group, n, max_q, rows):
+    su = Setup(qlin, "int8", 64, 32, 2, [n], [400])
+    q = bf(su.rows(2 * group))
+    su.cache.attend(qlin.KVBatch(i32([0, n]), i32([400]), i32(su.pages), rows, max_q, 400), q)
+    assert su.cache.poll_status() == qlin.QLIN_ERR_INVALID_ARG
