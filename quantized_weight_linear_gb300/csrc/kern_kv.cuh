@@ -61,9 +61,10 @@ struct KvSeq {
 __device__ __forceinline__ KvSeq kv_seq(const KvBatch& b, int seq) {
   KvSeq s;
   s.row0 = __ldg(b.q_start + seq);
-  s.n = __ldg(b.q_start + seq + 1) - s.row0;
+  const int end = __ldg(b.q_start + seq + 1);
   s.kv = __ldg(b.kv_len + seq);
-  if (s.row0 < 0 || s.n < 0 || s.n > b.max_q || s.row0 + s.n > b.total_q) {
+  s.n = (int)((uint32_t)end - (uint32_t)s.row0);  // wraps where the two are far out of range
+  if (s.row0 < 0 || end < s.row0 || end > b.total_q || s.n > b.max_q) {
     kv_report(b.status, kStatusInvalid);
     s.row0 = s.n = s.kv = 0;
   }

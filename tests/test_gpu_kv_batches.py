@@ -35,3 +35,22 @@ def test_one_sequence_with_more_tokens_than_said(qlin, group, n, max_q, rows):
     q = bf(su.rows(2 * group))
     su.cache.attend(qlin.KVBatch(i32([0, n]), i32([400]), i32(su.pages), rows, max_q, 400), q)
     assert su.cache.poll_status() == qlin.QLIN_ERR_INVALID_ARG
+
+
+BIG = 2 ** 31
+
+
+@pytest.mark.parametrize("q_start", [(BIG - 1, -BIG), (BIG - 3, -BIG + 1), (-BIG, BIG - 1), (-1, 0), (-1, 1), (0, BIG - 1), (1, 0),
+                                     (3, 5), (4, 5), (5, 5)])
+@pytest.mark.parametrize("group,max_q", [(2, 4), (20, 4)])
+def test_q_start_out_of_range(qlin, q_start, group, max_q):
+    """Sequences that are not rows 0..4 of the step, differences that wrap 32 bits among them."""
+    su = Setup(qlin, "int8", 64, 16, 1, [4], [40])
+    b = qlin.KVBatch(i32(q_start), i32([40]), i32(su.pages), 4, max_q, 40)
+    x = torch.zeros((4, 1, 64), dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros((4, group, 64), dtype=torch.bfloat16, device="cuda")
+    before = su.codes.clone()
+    for call in (lambda: su.cache.append(b, x, x, q=q), lambda: su.cache.read(b), lambda: su.cache.attend(b, q)):
+        call()
+        assert su.cache.poll_status() == qlin.QLIN_ERR_INVALID_ARG
+    assert torch.equal(before, su.codes)
