@@ -379,11 +379,20 @@ __device__ __forceinline__ bool find_block(const KvView& c, const KvBatch& b, in
   return true;
 }
 
-// One query item
+// One item for the whole batch: whether q_start falls (the items of a sequence that the search passes
+// over would not tell)
+__device__ __forceinline__ void check_order(const KvBatch& b, int lane) {
+  if (kv_falls(b, lane, 32)) kv_report(b.status, kStatusInvalid);
+}
+
+// One query item, and the one behind them
 template <int D>
 __device__ __forceinline__ void rotate_query(const AppendArgs& a, int64_t qi, int lane) {
   const int slabs = (a.q_elems + kQSlab - 1) / kQSlab;
-  if (qi >= (int64_t)a.batch.total_q * slabs) return;
+  if (qi >= (int64_t)a.batch.total_q * slabs) {
+    if (qi == (int64_t)a.batch.total_q * slabs) check_order(a.batch, lane);
+    return;
+  }
   const int t = (int)(qi / slabs), e0 = (int)(qi % slabs) * kQSlab, e1 = min(e0 + kQSlab, a.q_elems);
   const int d0 = (lane * 8) % D;  // the lane's elements of a head, every 256 / D heads
   const int off = partner_offset(a.rope, d0);
@@ -529,7 +538,10 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(ReadArgs a) {
     return;
   }
   const int64_t t = item - a.block_items;
-  if (t >= a.batch.total_q) return;
+  if (t >= a.batch.total_q) {
+    if (t == a.batch.total_q) check_order(a.batch, lane);
+    return;
+  }
   const int seq = kv_find_seq(a.batch, t, 1, 0, lane);
   const KvSeq s = kv_seq(a.batch, seq);
   if (s.n == 0 || t < s.row0 || t >= s.row0 + s.n || s.pos0 + (int)(t - s.row0) >= 0) return;
@@ -564,7 +576,7 @@ int64_t block_items(const KvView& c, const KvBatch& b) {
 int launch_kv_append(int code, int head_dim, const KvView& c, const KvBatch& b, const KvHeads& k, const KvHeads& v,
                      const KvHeads& q, int n_q_heads, uint16_t* q_out, const KvRope& r, void* stream) {
   AppendArgs a{c, b, k, v, q, q_out, r, n_q_heads * head_dim, block_items(c, b)};
-  const int64_t items = a.block_items * (head_dim / 64) + (int64_t)b.total_q * ((a.q_elems + kQSlab - 1) / kQSlab);
+  const int64_t items = a.block_items * (head_dim / 64) + (int64_t)b.total_q * ((a.q_elems + kQSlab - 1) / kQSlab) + 1;
   if (head_dim == 128)
     return launch_items(code == kKvInt8 ? kv_append_kernel<kKvInt8, 128> : kv_append_kernel<kKvE4m3, 128>, a, items, stream);
   return launch_items(code == kKvInt8 ? kv_append_kernel<kKvInt8, 64> : kv_append_kernel<kKvE4m3, 64>, a, items, stream);
@@ -573,7 +585,7 @@ int launch_kv_append(int code, int head_dim, const KvView& c, const KvBatch& b, 
 int launch_kv_read(int code, int head_dim, const KvView& c, const KvBatch& b, uint16_t* k_out, uint16_t* v_out,
                    void* stream) {
   ReadArgs a{c, b, k_out, v_out, block_items(c, b) / 2};
-  const int64_t items = a.block_items + b.total_q;
+  const int64_t items = a.block_items + b.total_q + 1;
   if (head_dim == 128)
     return launch_items(code == kKvInt8 ? kv_read_kernel<kKvInt8, 128> : kv_read_kernel<kKvE4m3, 128>, a, items, stream);
   return launch_items(code == kKvInt8 ? kv_read_kernel<kKvInt8, 64> : kv_read_kernel<kKvE4m3, 64>, a, items, stream);

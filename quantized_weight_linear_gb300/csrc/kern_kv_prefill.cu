@@ -350,6 +350,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const PreArgs p
       xt += yt;
     }
   }
+  // where q_start falls, the line and the items would not match: the sum of the tiles becomes negative
+  // (a return from here instead cost registers: a prompt chunk 1760 -> 2360 us)
+  if (__any_sync(0xffffffffu, kv_falls(a.batch, tid, kThreads))) {
+    kv_report(status, kStatusInvalid);
+    xt = -((int64_t)1 << 57);
+  }
   if (lane == 31) {
     scan[2 * warp] = x;
     scan[2 * warp + 1] = xt;
@@ -394,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const PreArgs p
   }
   __syncthreads();
   const int64_t ce = blockIdx.x < G ? split_start(blockIdx.x + 1, U, G) : U;
-  const int total = blockIdx.x < G ? (int)(sm.tiles_at[1] - sm.tiles_at[0]) : 0;  // tiles of this CTA
+  const int total = blockIdx.x < G && all_tiles >= 0 ? (int)(sm.tiles_at[1] - sm.tiles_at[0]) : 0;  // tiles of this CTA
   if (tid == 0) p.cuts[blockIdx.x].rows = 0;
   if (any_blind)
     for (int ub = blockIdx.x; ub < p.row_blocks; ub += (int)gridDim.x) {
@@ -609,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const PreArgs p
         if (g.part == 1)
           // the range ends before its tile t1, so its last tile's place is ce + n - t1 - 1
           p.cuts[blockIdx.x] = PreCut{w.b.rows, w.b.row0, w.head, w.b.s.row0,
-                                      (int)split_owner(ce + w.b.tiles - w.t1 - 1, U, G)};
+                                      (int)min(split_owner(ce + w.b.tiles - w.t1 - 1, U, G), G - 1)};
         mbar_arrive(&sm.seg_full[slot]);
       }
       more = w.next(p, lane);

@@ -54,3 +54,39 @@ def test_q_start_out_of_range(qlin, q_start, group, max_q):
         call()
         assert su.cache.poll_status() == qlin.QLIN_ERR_INVALID_ARG
     assert torch.equal(before, su.codes)
+
+
+@pytest.mark.parametrize("q_start,total,kv_lens,group", [
+    ((0, 2000, 300, 1500), 2000, (2000, 9000, 4000), 1),  # a search and a walk find different sequences
+    ((0, 2000, 300, 1500), 2000, (2000, 400, 9000), 4),
+    ((0, 40, 20, 60, 10, 100), 100, (40, 50, 60, 70, 200), 8),
+    ((5, 3, 1, 0), 8, (10, 20, 30), 1),
+    ((0, 8, 4, 8, 4, 8, 4, 8), 8, (9, 9, 9, 9, 9, 9, 9), 2),
+    (tuple(range(64)) + (0,), 64, (20,) * 64, 2),         # the last of many falls
+    (tuple(range(0, 4000, 10)) + (3000, 4000), 4000, (300,) * 401, 3),
+])
+@pytest.mark.parametrize("q", [True, False])
+def test_decreasing_q_start_is_reported(qlin, q_start, total, kv_lens, group, q):
+    """A q_start that falls is reported as a bad index by every call, which then makes no access that it
+    should not and does not hang; the workspace is good for the next call."""
+    D, page, n = 64, 64, len(kv_lens)
+    pages = -(-max(kv_lens) // page)
+    rng = torch.Generator(device="cuda").manual_seed(total)
+    codes = torch.randint(0, 256, (pages, 1, 2, page * D), generator=rng, device="cuda", dtype=torch.uint8)
+    cache = qlin.KVCache(codes, torch.rand((pages, 1, page // 16, 2), generator=rng, device="cuda") * 0.01)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").expand(n, pages).contiguous()
+    b = qlin.KVBatch(i32(q_start), i32(kv_lens), table, total, total, max(kv_lens))
+    x = torch.randn((total, 1, D), generator=rng, device="cuda").to(torch.bfloat16)
+    y = torch.randn((total, group, D), generator=rng, device="cuda").to(torch.bfloat16)
+    good = qlin.KVBatch(i32([0, total]), i32([max(kv_lens)]), table[:1], total, total, max(kv_lens))
+    want = cache.attend(good, y)
+    assert cache.poll_status() == 0
+    cache.read(b)
+    assert cache.poll_status() == qlin.QLIN_ERR_INVALID_ARG
+    cache.attend(b, y)
+    assert cache.poll_status() == qlin.QLIN_ERR_INVALID_ARG
+    assert torch.equal(cache.attend(good, y), want)
+    cache.append(b, x, x, q=y if q else None)
+    assert cache.poll_status() == qlin.QLIN_ERR_INVALID_ARG
+    cache.append(good, x, x)
+    assert cache.poll_status() == 0
