@@ -269,7 +269,9 @@ qlin_status qlin_poll_status(qlin_handle h, qlin_stream stream);
  *           QLIN_KV_INT8: byte = code + 128, code in -127..127
  *           QLIN_KV_E4M3: the bits of an fp8 e4m3 number
  *   scales  fp32 [n_pages][n_heads][page_tokens / 16][2]       (keys, values)
- * Memory that was never written may hold anything, NaN scales included.
+ * Memory that was never written may hold anything, NaN scales included.  Scales of what is held are
+ * not negative; qlin_kv_append writes none under 2^-60, and qlin_kv_attend takes a block whose value
+ * scale is under 2^-60 (0, in a cache from elsewhere) as values of 0.
  *
  * A batch is ragged: sequence b has the tokens q_start[b] <= t < q_start[b + 1] of a step,
  * which are the LAST ones of its kv_len[b] tokens: the i-th sits at position

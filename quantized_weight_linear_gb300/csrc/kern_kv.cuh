@@ -21,6 +21,15 @@ __host__ __device__ constexpr float kv_qmax_inv(int code) { return code == kKvIn
 // nothing the attention multiplies leaves the fp32 range on the small side
 constexpr float kKvMinScale = 8.673617379884035e-19f;
 
+// A value scale as the attention uses it: one under the smallest (0, in caches from elsewhere) has
+// neither logarithm nor reciprocal that the sums can take.  Such a block's values count as 0: its codes
+// are replaced by 0, which kv_no_values() tells, under half the smallest scale, whose reciprocal is exact
+// too.  Negative scales and NaN stay what they are and give NaN.
+__device__ __forceinline__ float kv_value_scale(float s) { return s >= 0.f && s < kKvMinScale ? 0.5f * kKvMinScale : s; }
+__device__ __forceinline__ bool kv_no_values(float inverse) { return inverse > 1.f / kKvMinScale; }
+// Four bytes of code 0
+__host__ __device__ constexpr uint32_t kv_zero_codes(int code) { return code == kKvInt8 ? 0x80808080u : 0u; }
+
 // Bytes of the K (or V) cell of one (block, head)
 template <int D>
 constexpr int kKvCellBytes = kKvBlock * D;

@@ -261,6 +261,14 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::kThreads, 1) kv_decode_kernel(c
     }
     float2 sc1 = scales_of(cell1);
     float ks = 1.f, lvs = 0.f, ivs = 1.f;
+    bool zeros = false;  // some block of the batch has no values
+    auto take = [&](const float2& sc) {
+      const float vs = kv_value_scale(sc.y);
+      ks = sc.x;
+      lvs = log2f(vs);
+      ivs = 1.f / vs;
+      zeros = __any_sync(0xffffffffu, kv_no_values(ivs));
+    };
 
     uint32_t qb[NT][KS][2];
     float rf[NT][2];
@@ -269,9 +277,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::kThreads, 1) kv_decode_kernel(c
       const int u = ws + j;
       if (j > 0 && (j & 7) == 0) {  // next batch of 8 units
         cell0 = cell1;
-        ks = sc1.x;
-        lvs = log2f(sc1.y);
-        ivs = 1.f / sc1.y;
+        take(sc1);
         cell1 = cell2;
         sc1 = scales_of(cell1);
         cell2 = cell_of(j + 16 + g);
@@ -313,11 +319,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::kThreads, 1) kv_decode_kernel(c
           }
         }
       }
-      if (j == 0) {  // after the first queries' loads went out
-        ks = sc0.x;
-        lvs = log2f(sc0.y);
-        ivs = 1.f / sc0.y;
-      }
+      if (j == 0) take(sc0);  // after the first queries' loads went out
       const int stage = j % C::kStages;
       const uint32_t phase = (uint32_t)(j / C::kStages) & 1u;
       const uint8_t* kc = ring + stage * C::kStage;
@@ -447,6 +449,16 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::kThreads, 1) kv_decode_kernel(c
             *v = kv_first_bytes(*v, have);
           }
           fence_proxy_async_smem();  // before the next copy into these bytes
+          __syncwarp();
+        }
+        if (zeros) {
+          for (int b = 0; b < kUnitBlocks; ++b) {
+            if (!kv_no_values(__shfl_sync(0xffffffffu, ivs, 4 * (j & 7) + b))) continue;
+            constexpr uint32_t z = kv_zero_codes(CODE);
+            uint4* v = reinterpret_cast<uint4*>(ring + stage * C::kStage + C::kK + b * C::kVCell);
+            for (int i = lane; i < D; i += 32) v[i] = make_uint4(z, z, z, z);
+          }
+          fence_proxy_async_smem();  // as above
           __syncwarp();
         }
         const uint8_t* vc = kc + C::kK + t * C::kVCell;

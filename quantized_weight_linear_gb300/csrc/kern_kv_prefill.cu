@@ -81,7 +81,7 @@ struct PreSmem {
   __align__(16) BlockInfo info[kSlots][kTileBlocks];
   __align__(16) Seg seg[kSegs];
   float2 other[kTileRows];            // M and L of the lane with the odd tiles
-  int tail[kSlots];                   // tokens of the tile that the sequence has
+  int tail[kSlots];                   // tokens of the tile that the sequence has, | its blocks without values << 16
   uint64_t op_full[kOps], op_empty[kOps], info_full[kSlots], info_empty[kSlots];
   uint64_t q_full[kSegs], q_empty, seg_full[kSegs], seg_empty[kSegs], s_full[2], p_full[2][2], o_full[2], o_empty[2], other_full;  // p_full: halves of 64 keys
   int start[3];  // row block, head, tile where the CTA's range begins
@@ -492,8 +492,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const PreArgs p
       ok = mbar_wait(&sm.info_empty[slot], ((uint32_t)(j / kSlots) & 1u) ^ 1u, status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      if (lane < kTileBlocks) sm.info[slot][lane] = BlockInfo{fmaxf(sc.x * a.scale, 1e-37f), log2f(sc.y), 1.f / sc.y, cell[0]};
-      if (lane == 0) sm.tail[slot] = h[0].tail;
+      const float vs = kv_value_scale(sc.y), ivs = 1.f / vs;
+      const unsigned none = __ballot_sync(0xffffffffu, kv_no_values(ivs)) & ((1u << kTileBlocks) - 1u);
+      if (lane < kTileBlocks) sm.info[slot][lane] = BlockInfo{fmaxf(sc.x * a.scale, 1e-37f), log2f(vs), ivs, cell[0]};
+      if (lane == 0) sm.tail[slot] = min(max(h[0].tail, 0), kTileKeys) | (int)none << 16;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.info_full[slot]);
       h[0] = h[1];
@@ -662,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const PreArgs p
                         : __ldcg(reinterpret_cast<const uint4*>(a.cache.codes + ((int64_t)cell + (values ? a.cache.page_blocks : 0)) *
                                                                                      kKvCellBytes<D>) + at);
       }
-      if (CODE == kKvE4m3) tail = sm.tail[slot];
+      tail = sm.tail[slot];
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.info_empty[slot]);
       return true;
@@ -681,9 +683,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const PreArgs p
         }
       } else {
         // e4m3: bytes behind the sequence's end may be NaN and are cleared (a NaN key is masked)
-        if (CODE == kKvE4m3 && tail < kTileKeys) {
+        if (CODE == kKvE4m3 ? tail != kTileKeys : tail > kTileKeys) {
+          constexpr uint32_t z = kv_zero_codes(CODE);
 #pragma unroll
-          for (int i = 0; i < kPieces; ++i) w[i] = kv_first_bytes(w[i], tail - block_at(i) * kKvBlock);
+          for (int i = 0; i < kPieces; ++i) {
+            if (CODE == kKvE4m3) w[i] = kv_first_bytes(w[i], (tail & 0xFFFF) - block_at(i) * kKvBlock);
+            if (tail >> (16 + block_at(i)) & 1) w[i] = make_uint4(z, z, z, z);
+          }
         }
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {

@@ -81,8 +81,8 @@ class Long:
             out += [c, s.reshape(self.H, -1, 1)[:, :self.T]]
         return out
 
-    def check(self, q_lens, kv_lens, q, o, lse, scale, rows=None, window=0, sinks=0):
-        """Compares the given rows (token, query head), all by default."""
+    def check(self, q_lens, kv_lens, q, o, lse, scale, rows=None, window=0, sinks=0, slack=0.0):
+        """Compares the given rows (sequence, token), all by default."""
         kc, ks, vc, vs = self.held()
         hq = q.shape[1]
         group = hq // self.H
@@ -111,7 +111,7 @@ class Long:
                 mag = ((x.abs() @ K.abs().T * scale) * seen[:, None]).amax(-1, keepdim=True)
                 codes = seen.double() @ vc[h, :kv].abs()
                 tol = 2.0 ** -8 * ref.abs() + (2.0 ** -10 + 2.0 ** -14 * (1 + mag)) * (p @ V.abs()) + \
-                    2.0 ** -31 * (p * vs[h, :kv, 0]).amax(-1, keepdim=True) * codes[:, None]
+                    2.0 ** -31 * (p * vs[h, :kv, 0]).amax(-1, keepdim=True) * codes[:, None] + slack
                 got = o[starts[b] + t, h * group:(h + 1) * group].double()
                 assert bool(torch.isfinite(got).all())
                 worst = max(worst, float(((got - ref).abs() / tol.clamp_min(1e-300)).max()))
@@ -155,3 +155,35 @@ def test_dominant_first_token(qlin, code, D, seqs, q_len, group):
     o, lse = su.cache.attend(su.batch(q_lens, kv_lens), q, return_lse=True)
     assert su.cache.poll_status() == 0
     su.check(q_lens, kv_lens, q, o, lse, scale, some_rows(q_lens, 6, seqs))
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("q_lens,group", [([1, 1, 1], 4), ([2, 1, 3], 5), ([17, 40, 9], 3), ([200, 90, 30], 2)])
+@pytest.mark.parametrize("which", ["values", "keys", "both", "all values", "tiny"])
+def test_scales_of_zero(qlin, code, D, q_lens, group, which):
+    """Blocks whose scale is 0, as an all-zero block of a cache from elsewhere may have it, with codes that
+    are not 0: keys and values of 0, exactly."""
+    T, H = 700, 2
+    su = Long(qlin, code, D, 48, H, T, seed=D + len(which))
+    some = torch.rand(su.scales.shape[:3], generator=su.g, device="cuda") < 0.4
+    if which in ("values", "both"):
+        su.scales[..., 1][some] = 0.0
+    if which in ("keys", "both"):
+        su.scales[..., 0][some.flip(0)] = 0.0
+    if which == "all values":
+        su.scales[..., 1] = 0.0
+    if which == "tiny":  # under 2^-60, down to numbers without a reciprocal in fp32
+        su.scales[..., 1][some] = torch.tensor([2.0 ** -61, 2.0 ** -100, 2.0 ** -140], device="cuda")[
+            torch.randint(0, 3, (int(some.sum()),), generator=su.g, device="cuda")]
+    kv_lens = [T, 333, 40]
+    q = bf(torch.randn(sum(q_lens), H * group, D, generator=su.g, device="cuda"))
+    o, lse = su.cache.attend(su.batch(q_lens, kv_lens), q, return_lse=True)
+    assert su.cache.poll_status() == 0
+    # (values of a scale under 2^-60 are themselves under 448 * 2^-60)
+    su.check(q_lens, kv_lens, q, o, lse, D ** -0.5, slack=448 * 2.0 ** -60 if which == "tiny" else 0.0)
+    if which == "all values":
+        assert not bool(o.any())
+    k, v = su.cache.read(su.batch([T], [T]))
+    held = su.held()
+    assert torch.equal(v.double(), (held[2] * held[3]).float().to(torch.bfloat16).double().transpose(0, 1))
