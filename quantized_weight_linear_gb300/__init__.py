@@ -532,7 +532,8 @@ class KVCache:
     semantics in include/qlin.h).
 
     codes uint8 [n_pages, n_heads, 2, page_tokens * head_dim], scales fp32
-    [n_pages, n_heads, page_tokens / 16, 2], both on the device; KVCache.empty allocates them.
+    [n_pages, n_heads, page_tokens / 16, 2], both on the device; KVCache.empty allocates them.  That
+    device has to be the current one in every call.
     A cache is not safe for concurrent calls from several threads.  Calls that share a workspace
     must not overlap on the GPU; caches whose calls follow one another (the layers of a model) can
     share one: KVCache(..., workspace=first.workspace)."""
@@ -556,12 +557,13 @@ class KVCache:
         # what every call needs, looked up once (a decoding step's calls are a few microseconds)
         self._lib, self._device, self._index = lib(), codes.device, codes.get_device()
         self._bf16, self._f32, self._empty, self._scale = torch.bfloat16, torch.float32, torch.empty, self.head_dim ** -0.5
-        self._raw_stream = torch._C._cuda_getCurrentRawStream
+        self._raw_stream, self._current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
         self._args = (HeadsStruct(), HeadsStruct(), HeadsStruct())  # k, v, q of the call being made
         self._arg_refs = tuple(ctypes.addressof(x) for x in self._args)
         self.struct = KvCacheStruct(_KV_CODES[code], self.n_pages, self.n_heads, self.head_dim, self.page_tokens,
                                     codes.data_ptr(), scales.data_ptr())
         self.ref = ctypes.addressof(self.struct)
+        stream = self._on(stream)
         n = ctypes.c_size_t()
         _check(lib().qlin_kv_workspace_bytes(self.ref, ctypes.byref(n)), "qlin_kv_workspace_bytes")
         self.ws_bytes = n.value
@@ -573,7 +575,7 @@ class KVCache:
             raise ValueError("workspace too small")
         if scales.get_device() != self._index or workspace.get_device() != self._index:
             raise ValueError("codes, scales and workspace must be on one device")
-        _check(lib().qlin_kv_init_workspace(self.ws, n.value, self._on(stream)), "qlin_kv_init_workspace")
+        _check(lib().qlin_kv_init_workspace(self.ws, n.value, stream), "qlin_kv_init_workspace")
 
     @classmethod
     def empty(cls, n_pages: int, n_heads: int, head_dim: int, page_tokens: int = 64, code: str = "int8", device="cuda",
@@ -604,8 +606,16 @@ class KVCache:
         return x
 
     def _on(self, stream):
-        """The stream's handle; by default the current one of the cache's device."""
-        return self._raw_stream(self._index) if stream is None else _stream(stream)
+        """The stream's handle; by default the current one of the cache's device, which has to be the
+        current device: the library launches on that one."""
+        if self._current_device() != self._index:
+            raise ValueError(f"the current device is cuda:{self._current_device()}, the cache is on cuda:{self._index}: "
+                             f"call it under torch.cuda.device({self._index})")
+        if stream is None:
+            return self._raw_stream(self._index)
+        if getattr(stream, "device_index", self._index) != self._index:
+            raise ValueError("the stream is on another device than the cache")
+        return _stream(stream)
 
     def _same_device(self, x, what):
         if x.index != self._index:
