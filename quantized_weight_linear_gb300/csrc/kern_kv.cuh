@@ -86,12 +86,10 @@ __device__ __forceinline__ KvSeq kv_seq(const KvBatch& b, int seq) {
   return s;
 }
 
-// Whether q_start falls somewhere among the entries s, s + step, ... (and their next ones).  The searches
-// below, and the walks that stand for them, give one answer only where it does not.
-__device__ __forceinline__ bool kv_falls(const KvBatch& b, int s, int step) {
-  bool falls = false;
-  for (; s < b.n_seqs; s += step) falls |= __ldg(b.q_start + s + 1) < __ldg(b.q_start + s);
-  return falls;
+// Whether q_start falls after entry s.  The searches below, and the walks that stand for them, give one
+// answer only where it does nowhere.
+__device__ __forceinline__ bool kv_falls(const KvBatch& b, int s) {
+  return s < b.n_seqs && __ldg(b.q_start + s + 1) < __ldg(b.q_start + s);
 }
 
 // Largest seq with first(seq) <= u, for the non-decreasing first(s) = q_start[s] / div + mul * s

@@ -379,18 +379,18 @@ __device__ __forceinline__ bool find_block(const KvView& c, const KvBatch& b, in
   return true;
 }
 
-// One item for the whole batch: whether q_start falls (the items of a sequence that the search passes
-// over would not tell)
-__device__ __forceinline__ void check_order(const KvBatch& b, int lane) {
-  if (kv_falls(b, lane, 32)) kv_report(b.status, kStatusInvalid);
+// An item for every 32 sequences: whether q_start falls (the items of a sequence that the search passes
+// over would not tell; where every sequence has its item, the launch has none of these)
+__device__ __forceinline__ void check_order(const KvBatch& b, int64_t item, int lane) {
+  if (item * 32 < b.n_seqs && kv_falls(b, (int)item * 32 + lane)) kv_report(b.status, kStatusInvalid);
 }
 
-// One query item, and the one behind them
+// One query item, or one of those behind them
 template <int D>
 __device__ __forceinline__ void rotate_query(const AppendArgs& a, int64_t qi, int lane) {
   const int slabs = (a.q_elems + kQSlab - 1) / kQSlab;
   if (qi >= (int64_t)a.batch.total_q * slabs) {
-    if (qi == (int64_t)a.batch.total_q * slabs) check_order(a.batch, lane);
+    if (a.batch.max_q > 1) check_order(a.batch, qi - (int64_t)a.batch.total_q * slabs, lane);
     return;
   }
   const int t = (int)(qi / slabs), e0 = (int)(qi % slabs) * kQSlab, e1 = min(e0 + kQSlab, a.q_elems);
@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(ReadArgs a) {
   }
   const int64_t t = item - a.block_items;
   if (t >= a.batch.total_q) {
-    if (t == a.batch.total_q) check_order(a.batch, lane);
+    if (a.batch.max_q > 1) check_order(a.batch, t - a.batch.total_q, lane);
     return;
   }
   const int seq = kv_find_seq(a.batch, t, 1, 0, lane);
@@ -566,6 +566,7 @@ int launch_items(void (*kernel)(Args), const Args& a, int64_t items, void* strea
   return (int)cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
+int order_items(const KvBatch& b) { return b.max_q > 1 ? (b.n_seqs + 31) / 32 : 0; }
 int64_t block_items(const KvView& c, const KvBatch& b) {
   const int64_t blocks = b.max_q <= 1 ? b.n_seqs : (int64_t)b.total_q / kKvBlock + 2 * (int64_t)b.n_seqs;
   return blocks * c.n_heads * 2;
@@ -576,7 +577,7 @@ int64_t block_items(const KvView& c, const KvBatch& b) {
 int launch_kv_append(int code, int head_dim, const KvView& c, const KvBatch& b, const KvHeads& k, const KvHeads& v,
                      const KvHeads& q, int n_q_heads, uint16_t* q_out, const KvRope& r, void* stream) {
   AppendArgs a{c, b, k, v, q, q_out, r, n_q_heads * head_dim, block_items(c, b)};
-  const int64_t items = a.block_items * (head_dim / 64) + (int64_t)b.total_q * ((a.q_elems + kQSlab - 1) / kQSlab) + 1;
+  const int64_t items = a.block_items * (head_dim / 64) + (int64_t)b.total_q * ((a.q_elems + kQSlab - 1) / kQSlab) + order_items(b);
   if (head_dim == 128)
     return launch_items(code == kKvInt8 ? kv_append_kernel<kKvInt8, 128> : kv_append_kernel<kKvE4m3, 128>, a, items, stream);
   return launch_items(code == kKvInt8 ? kv_append_kernel<kKvInt8, 64> : kv_append_kernel<kKvE4m3, 64>, a, items, stream);
@@ -585,7 +586,7 @@ int launch_kv_append(int code, int head_dim, const KvView& c, const KvBatch& b, 
 int launch_kv_read(int code, int head_dim, const KvView& c, const KvBatch& b, uint16_t* k_out, uint16_t* v_out,
                    void* stream) {
   ReadArgs a{c, b, k_out, v_out, block_items(c, b) / 2};
-  const int64_t items = a.block_items + b.total_q + 1;
+  const int64_t items = a.block_items + b.total_q + order_items(b);
   if (head_dim == 128)
     return launch_items(code == kKvInt8 ? kv_read_kernel<kKvInt8, 128> : kv_read_kernel<kKvE4m3, 128>, a, items, stream);
   return launch_items(code == kKvInt8 ? kv_read_kernel<kKvInt8, 64> : kv_read_kernel<kKvE4m3, 64>, a, items, stream);

@@ -352,7 +352,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const PreArgs p
   }
   // where q_start falls, the line and the items would not match: the sum of the tiles becomes negative
   // (a return from here instead cost registers: a prompt chunk 1760 -> 2360 us)
-  if (__any_sync(0xffffffffu, kv_falls(a.batch, tid, kThreads))) {
+  bool falls = false;
+  for (int s = tid; s < a.batch.n_seqs; s += kThreads) falls |= kv_falls(a.batch, s);
+  if (__any_sync(0xffffffffu, falls)) {
     kv_report(status, kStatusInvalid);
     xt = -((int64_t)1 << 57);
   }
@@ -371,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const PreArgs p
     all_tiles += scan[2 * w + 1];
   }
   // at least two tiles a CTA
-  const int64_t G = max((int64_t)1, min((int64_t)gridDim.x, U / (kItemCost + 2)));
+  const int64_t G = all_tiles < 0 ? 0 : max((int64_t)1, min((int64_t)gridDim.x, U / (kItemCost + 2)));
   if (blockIdx.x < G) {
     for (int e = 0; e < 2; ++e) {  // the range's begin and end
       const int64_t at = split_start(blockIdx.x + e, U, G);
@@ -400,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const PreArgs p
   }
   __syncthreads();
   const int64_t ce = blockIdx.x < G ? split_start(blockIdx.x + 1, U, G) : U;
-  const int total = blockIdx.x < G && all_tiles >= 0 ? (int)(sm.tiles_at[1] - sm.tiles_at[0]) : 0;  // tiles of this CTA
+  const int total = blockIdx.x < G ? (int)(sm.tiles_at[1] - sm.tiles_at[0]) : 0;  // tiles of this CTA
   if (tid == 0) p.cuts[blockIdx.x].rows = 0;
   if (any_blind)
     for (int ub = blockIdx.x; ub < p.row_blocks; ub += (int)gridDim.x) {

@@ -77,6 +77,7 @@ def test_decreasing_q_start_is_reported(qlin, q_start, total, kv_lens, group, q)
     table = torch.arange(pages, dtype=torch.int32, device="cuda").expand(n, pages).contiguous()
     b = qlin.KVBatch(i32(q_start), i32(kv_lens), table, total, total, max(kv_lens))
     x = torch.randn((total, 1, D), generator=rng, device="cuda").to(torch.bfloat16)
+    one = qlin.KVBatch(i32(q_start), i32(kv_lens), table, total, 1, max(kv_lens))  # said to have single tokens
     y = torch.randn((total, group, D), generator=rng, device="cuda").to(torch.bfloat16)
     good = qlin.KVBatch(i32([0, total]), i32([max(kv_lens)]), table[:1], total, total, max(kv_lens))
     want = cache.attend(good, y)
@@ -88,5 +89,8 @@ def test_decreasing_q_start_is_reported(qlin, q_start, total, kv_lens, group, q)
     assert torch.equal(cache.attend(good, y), want)
     cache.append(b, x, x, q=y if q else None)
     assert cache.poll_status() == qlin.QLIN_ERR_INVALID_ARG
+    for call in (lambda: cache.read(one), lambda: cache.attend(one, y), lambda: cache.append(one, x, x, q=y if q else None)):
+        call()
+        assert cache.poll_status() == qlin.QLIN_ERR_INVALID_ARG
     cache.append(good, x, x)
     assert cache.poll_status() == 0
