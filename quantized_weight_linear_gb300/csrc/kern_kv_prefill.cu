@@ -632,6 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const PreArgs p
     const bool values = warp >= 8;
     const int ct = tid & 127;
     constexpr int kPieces = kTileKeys * D / 16 / 128;
+    constexpr uint32_t kZero = kv_zero_codes(CODE);
     // Key pieces: four lanes take 64 bytes of a key, so that the eight lanes of a store's phase are
     // two neighbouring keys, whose swizzles differ in the lowest bit: all banks, no conflicts.
     constexpr int kHalves = D / 64;
@@ -666,7 +667,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const PreArgs p
                         : __ldcg(reinterpret_cast<const uint4*>(a.cache.codes + ((int64_t)cell + (values ? a.cache.page_blocks : 0)) *
                                                                                      kKvCellBytes<D>) + at);
       }
-      tail = sm.tail[slot];
+      // blocks without values: cleared here, or with the tail's bytes (each where it measured better: as below
+      // for both codes a prompt chunk of int8 takes 1780 us instead of 1747, as here a window prompt of e4m3
+      // 233 instead of 209)
+      if constexpr (CODE == kKvE4m3) {
+        tail = sm.tail[slot];
+      } else if (const int none = sm.tail[slot] >> 16; values && none) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+          if (none >> block_at(i) & 1) w[i] = make_uint4(kZero, kZero, kZero, kZero);
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.info_empty[slot]);
       return true;
@@ -685,12 +695,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const PreArgs p
         }
       } else {
         // e4m3: bytes behind the sequence's end may be NaN and are cleared (a NaN key is masked)
-        if (CODE == kKvE4m3 ? tail != kTileKeys : tail > kTileKeys) {
-          constexpr uint32_t z = kv_zero_codes(CODE);
+        if (CODE == kKvE4m3 && tail != kTileKeys) {
 #pragma unroll
           for (int i = 0; i < kPieces; ++i) {
-            if (CODE == kKvE4m3) w[i] = kv_first_bytes(w[i], (tail & 0xFFFF) - block_at(i) * kKvBlock);
-            if (tail >> (16 + block_at(i)) & 1) w[i] = make_uint4(z, z, z, z);
+            w[i] = kv_first_bytes(w[i], (tail & 0xFFFF) - block_at(i) * kKvBlock);
+            if (tail >> (16 + block_at(i)) & 1) w[i] = make_uint4(kZero, kZero, kZero, kZero);
           }
         }
 #pragma unroll
