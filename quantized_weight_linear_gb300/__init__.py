@@ -527,6 +527,21 @@ class KVBatch:
         self.ref = ctypes.addressof(self.struct)
 
 
+class KVWorkspace:
+    """Device workspace of cache calls (status word, counters, partial results) in a uint8 tensor: cleared
+    when it is made, on `stream`, and not by the caches that are given it."""
+
+    def __init__(self, memory, stream=None):
+        import torch
+        self.memory, self.index = memory, memory.get_device()
+        if torch._C._cuda_getDevice() != self.index:
+            raise ValueError("the workspace is not on the current device")
+        self.ptr = memory.data_ptr() + (-memory.data_ptr()) % 256
+        self.nbytes = memory.data_ptr() + memory.numel() - self.ptr
+        on = torch._C._cuda_getCurrentRawStream(self.index) if stream is None else _stream(stream)
+        _check(lib().qlin_kv_init_workspace(self.ptr, max(self.nbytes, 0), on), "qlin_kv_init_workspace")
+
+
 class KVCache:
     """A paged 8-bit key/value cache of one layer and the attention over it (layouts and
     semantics in include/qlin.h).
@@ -536,7 +551,8 @@ class KVCache:
     device has to be the current one in every call.
     A cache is not safe for concurrent calls from several threads.  Calls that share a workspace
     must not overlap on the GPU; caches whose calls follow one another (the layers of a model) can
-    share one: KVCache(..., workspace=first.workspace)."""
+    share one: KVCache(..., workspace=first.workspace), a KVWorkspace.  Their status is shared too.  A
+    plain uint8 tensor is taken as fresh memory and cleared."""
 
     def __init__(self, codes, scales, code: str = "int8", workspace=None, stream=None):
         import torch
@@ -563,19 +579,22 @@ class KVCache:
         self.struct = KvCacheStruct(_KV_CODES[code], self.n_pages, self.n_heads, self.head_dim, self.page_tokens,
                                     codes.data_ptr(), scales.data_ptr())
         self.ref = ctypes.addressof(self.struct)
-        stream = self._on(stream)
+        self._on(stream)  # refuses another device's
         n = ctypes.c_size_t()
         _check(lib().qlin_kv_workspace_bytes(self.ref, ctypes.byref(n)), "qlin_kv_workspace_bytes")
         self.ws_bytes = n.value
         if workspace is None:
             workspace = torch.empty(n.value + 256, dtype=torch.uint8, device=codes.device)
-        self.workspace = workspace
-        self.ws = workspace.data_ptr() + (-workspace.data_ptr()) % 256
-        if self.ws + n.value > workspace.data_ptr() + workspace.numel():
-            raise ValueError("workspace too small")
-        if scales.get_device() != self._index or workspace.get_device() != self._index:
+        if scales.get_device() != self._index or (workspace.index if isinstance(workspace, KVWorkspace) else
+                                                  workspace.get_device()) != self._index:
             raise ValueError("codes, scales and workspace must be on one device")
-        _check(lib().qlin_kv_init_workspace(self.ws, n.value, stream), "qlin_kv_init_workspace")
+        if not isinstance(workspace, KVWorkspace):
+            if (-workspace.data_ptr()) % 256 + n.value > workspace.numel():
+                raise ValueError("workspace too small")
+            workspace = KVWorkspace(workspace, stream)
+        if workspace.nbytes < n.value:
+            raise ValueError("workspace too small")
+        self.workspace, self.ws = workspace, workspace.ptr
 
     @classmethod
     def empty(cls, n_pages: int, n_heads: int, head_dim: int, page_tokens: int = 64, code: str = "int8", device="cuda",

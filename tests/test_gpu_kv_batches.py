@@ -94,3 +94,16 @@ def test_decreasing_q_start_is_reported(qlin, q_start, total, kv_lens, group, q)
         assert cache.poll_status() == qlin.QLIN_ERR_INVALID_ARG
     cache.append(good, x, x)
     assert cache.poll_status() == 0
+
+
+def test_errors_outlive_a_cache_on_the_same_workspace(qlin):
+    """A bad index that nobody has polled for is still there after another layer's cache took the workspace."""
+    su = Setup(qlin, "int8", 64, 16, 1, [1], [40])
+    pages = su.pages.copy()
+    pages[0, 2] = -5
+    q = bf(su.rows(2))
+    su.cache.attend(su.make_batch([1], pages=pages), q)
+    second = qlin.KVCache(su.codes.clone(), su.scales.clone(), workspace=su.cache.workspace)
+    assert second.poll_status() == qlin.QLIN_ERR_INVALID_ARG
+    assert torch.equal(second.attend(su.batch, q), su.cache.attend(su.batch, q))
+    su.ok()

@@ -104,3 +104,31 @@ def test_a_stream_of_another_device_is_refused(world):
         with pytest.raises(ValueError, match="stream"):
             call()
     assert world.lib.calls == []
+
+
+def test_a_shared_workspace_is_cleared_once(world):
+    first = world.cache(0)
+    assert world.lib.calls.count("qlin_kv_init_workspace") == 1
+    second = world.cache(0, workspace=first.workspace)
+    assert second.ws == first.ws and world.lib.calls.count("qlin_kv_init_workspace") == 1
+    world.cache(0, workspace=Tensor((1 << 20,), torch.uint8, 0))  # fresh memory
+    assert world.lib.calls.count("qlin_kv_init_workspace") == 2
+
+
+def test_workspaces_that_do_not_fit_are_refused(world):
+    def needs(c, n):  # what the library asks for
+        n._obj.value = 4096
+        return 0
+    world.lib.qlin_kv_workspace_bytes = needs
+    for memory in (Tensor((4000,), torch.uint8, 0), world.qlin.KVWorkspace(Tensor((4095,), torch.uint8, 0))):
+        with pytest.raises(ValueError, match="too small"):
+            world.cache(0, workspace=memory)
+    with pytest.raises(ValueError, match="current device"):
+        world.qlin.KVWorkspace(Tensor((5000,), torch.uint8, 1))
+    world.device = 1
+    there = world.qlin.KVWorkspace(Tensor((5000,), torch.uint8, 1))
+    world.device = 0
+    for memory in (Tensor((5000,), torch.uint8, 1), there):
+        with pytest.raises(ValueError, match="one device"):
+            world.cache(0, workspace=memory)
+    world.cache(0, workspace=Tensor((4096,), torch.uint8, 0))
