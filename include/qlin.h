@@ -288,7 +288,8 @@ qlin_status qlin_poll_status(qlin_handle h, qlin_stream stream);
  * as QLIN_ERR_INVALID_ARG by qlin_kv_poll_status, and the outputs concerned are unspecified.
  *
  * Supported: head_dim 64 or 128, page_tokens a multiple of 16, at most 2048 sequences a step,
- * query heads a multiple of the key/value heads.  Calls on one workspace must not overlap on
+ * query heads a multiple of the key/value heads; attention: fewer than 2^31 rows (tokens x query
+ * heads of a key/value head) in a sequence and 2^31 blocks of 256 of them in a step.  Calls on one workspace must not overlap on
  * the GPU.  All pointers 16-byte aligned except the index arrays (4-byte) and the workspace
  * (256-byte). */
 typedef enum { QLIN_KV_INT8 = 1, QLIN_KV_E4M3 = 2 } qlin_kv_code;

@@ -554,8 +554,10 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(ReadArgs a) {
 template <typename Args>
 int launch_items(void (*kernel)(Args), const Args& a, int64_t items, void* stream) {
   if (items <= 0) return 0;
+  const int64_t ctas = (items + kThreads / 32 - 1) / (kThreads / 32);
+  if (ctas > INT32_MAX) return (int)cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((items + kThreads / 32 - 1) / (kThreads / 32)));
+  cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = (cudaStream_t)stream;
   cudaLaunchAttribute at{};

@@ -47,6 +47,7 @@ namespace {
 constexpr int kThreads = 640;
 constexpr int kTileRows = 128;
 constexpr int kCtaRows = 2 * kTileRows;
+static_assert(kCtaRows == kKvPrefillRows, "row blocks");
 constexpr int kTileKeys = 128;
 constexpr int kTileBlocks = kTileKeys / kKvBlock;
 constexpr int kSlots = 4;  // tiles in the table
@@ -416,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const PreArgs p
     }
   if (total == 0) return;
   if (smem_u32(smem_raw) & 1023u) {  // the operands' swizzle needs it; dynamic shared memory starts so
-    if (tid == 0) kv_report(status, kStatusTimeout);
+    if (tid == 0) kv_report(status, kStatusInternal);
     return;
   }
   if (warp == 1) {
@@ -1207,8 +1208,7 @@ size_t kv_prefill_partial_bytes(int head_dim, int sms) {
 }
 
 int launch_kv_prefill(int code, int head_dim, const KvAttendArgs& a, int rows, int sms, void* stream) {
-  const int64_t blocks = (int64_t)a.batch.total_q * a.group / kCtaRows + a.batch.n_seqs;
-  if (blocks * a.cache.n_heads > INT32_MAX) return (int)cudaErrorInvalidValue;
+  const int64_t blocks = (int64_t)a.batch.total_q * a.group / kCtaRows + a.batch.n_seqs;  // (the host checked that it fits)
   const PreArgs p{a, (PreCut*)a.partials, (float*)((uint8_t*)a.partials + kCutBytes), (int)blocks};
   if (head_dim == 128) return code == kKvInt8 ? launch_rows<kKvInt8, 128>(p, rows, sms, stream) : launch_rows<kKvE4m3, 128>(p, rows, sms, stream);
   return code == kKvInt8 ? launch_rows<kKvInt8, 64>(p, rows, sms, stream) : launch_rows<kKvE4m3, 64>(p, rows, sms, stream);

@@ -147,6 +147,11 @@ qlin_status qlin_kv_attend(const qlin_kv_cache* c, const qlin_kv_batch* b, const
   const int64_t most = (int64_t)std::min(a.batch.max_q, a.batch.total_q) * a.group;
   // (a step may have rows that no sequence has: total_q says nothing of a sequence's rows)
   const int64_t least = uniform ? most : 1;
+  // rows of a sequence, and (row block, head) items of a step, are counted in 32 bits
+  if (most > INT32_MAX ||
+      (most > kKvDecodeRows &&
+       ((int64_t)a.batch.total_q * a.group / kKvPrefillRows + a.batch.n_seqs) * a.cache.n_heads > INT32_MAX))
+    return QLIN_ERR_UNSUPPORTED;
   a.min_rows = 1;
   a.max_rows = most <= kKvDecodeRows ? INT32_MAX : kKvDecodeRows;
   int e = 0;

@@ -5,8 +5,8 @@
 
 namespace qlin {
 
-// device status word: a bad index in the batch's device arrays
-constexpr int kStatusInvalid = 1;
+// device status word: a bad index in the batch's device arrays; a fault of the library's own
+constexpr int kStatusInvalid = 1, kStatusInternal = 3;
 
 constexpr int kKvBlock = 16;      // tokens that share a scale
 constexpr int kKvMaxSeqs = 2048;  // sequences of a step
@@ -64,6 +64,7 @@ int launch_kv_read(int code, int head_dim, const KvView& c, const KvBatch& b, ui
 constexpr int kKvDecodeRows = 16;  // up to so many rows: kern_kv_decode.cu, more: kern_kv_prefill.cu
 // rows: most query rows per key/value head of a sequence
 int launch_kv_decode(int code, int head_dim, const KvAttendArgs& a, int rows, int sms, void* stream);
+constexpr int kKvPrefillRows = 256;  // rows of a row block of the latter
 size_t kv_prefill_partial_bytes(int head_dim, int sms);
 int launch_kv_prefill(int code, int head_dim, const KvAttendArgs& a, int rows, int sms, void* stream);
 
