@@ -94,13 +94,14 @@ class Long:
                 continue
             t = torch.tensor(tokens, device="cuda")
             pos = kv - n + t
-            j = torch.arange(kv, device="cuda")
+            have = max(kv, 1)  # (a sequence of no tokens sees nothing of one)
+            j = torch.arange(have, device="cuda")
             seen = j <= pos[:, None]
             if window:
                 seen &= (j > pos[:, None] - window) | (j < sinks)
             for h in range(self.H):
                 x = q[starts[b] + t, h * group:(h + 1) * group].double()  # [t, g, D]
-                K, V = kc[h, :kv] * ks[h, :kv], vc[h, :kv] * vs[h, :kv]
+                K, V = kc[h, :have] * ks[h, :have], vc[h, :have] * vs[h, :have]
                 w = (x @ K.T * scale).masked_fill(~seen[:, None], -torch.inf)
                 m = w.amax(-1, keepdim=True)
                 none = torch.isneginf(m)
@@ -109,9 +110,9 @@ class Long:
                 p = torch.where(none, torch.zeros_like(p), p / torch.where(none, torch.ones_like(total), total))
                 ref = p @ V
                 mag = ((x.abs() @ K.abs().T * scale) * seen[:, None]).amax(-1, keepdim=True)
-                codes = seen.double() @ vc[h, :kv].abs()
+                codes = seen.double() @ vc[h, :have].abs()
                 tol = 2.0 ** -8 * ref.abs() + (2.0 ** -10 + 2.0 ** -14 * (1 + mag)) * (p @ V.abs()) + \
-                    2.0 ** -31 * (p * vs[h, :kv, 0]).amax(-1, keepdim=True) * codes[:, None] + slack
+                    2.0 ** -31 * (p * vs[h, :have, 0]).amax(-1, keepdim=True) * codes[:, None] + slack
                 got = o[starts[b] + t, h * group:(h + 1) * group].double()
                 assert bool(torch.isfinite(got).all())
                 worst = max(worst, float(((got - ref).abs() / tol.clamp_min(1e-300)).max()))
@@ -187,3 +188,89 @@ def test_scales_of_zero(qlin, code, D, q_lens, group, which):
     k, v = su.cache.read(su.batch([T], [T]))
     held = su.held()
     assert torch.equal(v.double(), (held[2] * held[3]).float().to(torch.bfloat16).double().transpose(0, 1))
+
+
+# Work enough that every warp (CTA) goes round its rings and tables, takes several batches of lookups and
+# several items, and joins them over all CTAs
+
+def run(qlin, code, D, page, H, group, q_lens, kv_lens, window=0, sinks=0, seed=0, pick=None):
+    su = Long(qlin, code, D, page, H, max(kv_lens), seed)
+    q = bf(torch.randn(sum(q_lens), H * group, D, generator=su.g, device="cuda") * 1.5)
+    batch = su.batch(q_lens, kv_lens)
+    o, lse = su.cache.attend(batch, q, window=window, sinks=sinks, return_lse=True)
+    assert su.cache.poll_status() == 0
+    rows = None if pick is None else some_rows(q_lens, pick, seed)
+    su.check(q_lens, kv_lens, q, o, lse, D ** -0.5, rows, window, sinks)
+    again = su.cache.attend(batch, q, window=window, sinks=sinks)
+    assert su.cache.poll_status() == 0 and torch.equal(o, again)
+
+
+def lengths(seed, n, lo, hi):
+    return [int(x) for x in np.random.default_rng(seed).integers(lo, hi, n)]
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("group", [4, 12])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (2900, 20)])
+def test_decode_many_units_a_warp(qlin, code, D, group, window, sinks):
+    """64 sequences of 3000 to 5000 tokens, 8 heads: some 35 units of 64 tokens for each of 900 warps (rings of
+    two or four stages, lookups of eight units), items that end anywhere in them."""
+    run(qlin, code, D, 64, 8, group, [1] * 64, lengths(D + group, 64, 3000, 5000), window, sinks, seed=group, pick=24)
+
+
+@pytest.mark.parametrize("code,D,group", [("int8", 128, 4), ("e4m3", 128, 16), ("int8", 64, 16), ("e4m3", 64, 1)])
+def test_decode_item_over_all_ctas(qlin, code, D, group):
+    """One head of one sequence of 210000 tokens: its parts are joined over all CTAs."""
+    run(qlin, code, D, 128, 1, group, [1], [210007], seed=group)
+
+
+@pytest.mark.parametrize("n", [193, 700, 2048])
+@pytest.mark.parametrize("group,q_len", [(4, 1), (5, 3)])
+def test_decode_many_sequences(qlin, n, group, q_len):
+    """More sequences than a CTA has threads, up to the most: lengths from none on."""
+    run(qlin, "int8", 64, 16, 2, group, [q_len] * n, lengths(n, n, 0, 300), seed=n, pick=200)
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (700, 20)])
+@pytest.mark.parametrize("most", [30, 160])
+def test_prompts_many_items_a_cta(qlin, code, D, window, sinks, most):
+    """Up to 120 rows a head in every sequence (the variant for few rows), or up to 640 beside few: some five
+    items and tens of key tiles a CTA, items of one and of two row tiles in turn."""
+    n = 100 if most == 30 else 60
+    q_lens = lengths(D, n, 5, most)
+    kv_lens = [q + x for q, x in zip(q_lens, lengths(most, n, 500, 4500))]
+    run(qlin, code, D, 48, 8, 4, q_lens, kv_lens, window, sinks, seed=most, pick=10)
+
+
+@pytest.mark.parametrize("n,q_len,group", [(900, 20, 1), (2048, 40, 2), (2048, 9, 2)])
+def test_prompts_many_row_blocks(qlin, n, q_len, group):
+    """More row blocks than a CTA has threads."""
+    q_lens = lengths(q_len, n, q_len - 3, q_len + 1)
+    run(qlin, "int8", 64, 32, 1, group, q_lens, [max(q + x, 0) for q, x in zip(q_lens, lengths(n, n, -30, 400))],
+        seed=q_len, pick=150)
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+def test_append_many_sequences(qlin, code):
+    from test_gpu_kv import run_append
+    n = 2048
+    q = lengths(1, n, 0, 4)
+    run_append(qlin, code, 64, 16, 1, q, [max(a + b, 0) for a, b in zip(q, lengths(2, n, -2, 20))], 64, hq=1)
+    run_append(qlin, code, 64, 16, 1, [1] * n, lengths(3, n, 0, 20), 64, hq=1)
+
+
+@pytest.mark.parametrize("qscale", [2.0 ** 16, 2.0 ** 20, 2.0 ** 23])
+@pytest.mark.parametrize("q_lens,group", [([1, 1], 4), ([3, 4], 4), ([30, 9], 2), ([150, 40], 2)])
+def test_scores_far_out(qlin, qscale, q_lens, group):
+    """Scores so large that fp32 rounds them by whole powers of two of a weight: an output is one value or a
+    mixture of a few, and stays among the values."""
+    for code, D in (("int8", 64), ("e4m3", 128)):
+        su = Long(qlin, code, D, 32, 2, 900, seed=D)
+        q = bf(torch.randn(sum(q_lens), 2 * group, D, generator=su.g, device="cuda") * qscale)
+        o = su.cache.attend(su.batch(q_lens, [900, 500]), q)
+        assert su.cache.poll_status() == 0
+        _, _, vc, vs = su.held()
+        assert bool(torch.isfinite(o).all()) and float(o.abs().max()) <= float((vc * vs).abs().max()) * 1.01
