@@ -527,6 +527,16 @@ class KVBatch:
         self.ref = ctypes.addressof(self.struct)
 
 
+def _allocate_on(stream, make):
+    """make() with its tensors belonging to `stream` (an int handle, a torch stream, or None: the current one):
+    memory that kernels queued elsewhere still use is not handed out to it."""
+    import torch
+    if stream is None:
+        return make()
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
+        return make()
+
+
 class KVWorkspace:
     """Device workspace of cache calls (status word, counters, partial results) in a uint8 tensor: cleared
     when it is made, on `stream`, and not by the caches that are given it."""
@@ -548,7 +558,8 @@ class KVCache:
 
     codes uint8 [n_pages, n_heads, 2, page_tokens * head_dim], scales fp32
     [n_pages, n_heads, page_tokens / 16, 2], both on the device; KVCache.empty allocates them.  That
-    device has to be the current one in every call.
+    device has to be the current one in every call.  A call runs on `stream` (default: the current one),
+    to which the tensors that it makes belong; the stream waits for the caller's inputs if the caller says so.
     A cache is not safe for concurrent calls from several threads.  Calls that share a workspace
     must not overlap on the GPU; caches whose calls follow one another (the layers of a model) can
     share one: KVCache(..., workspace=first.workspace), a KVWorkspace.  Their status is shared too.  A
@@ -584,7 +595,7 @@ class KVCache:
         _check(lib().qlin_kv_workspace_bytes(self.ref, ctypes.byref(n)), "qlin_kv_workspace_bytes")
         self.ws_bytes = n.value
         if workspace is None:
-            workspace = torch.empty(n.value + 256, dtype=torch.uint8, device=codes.device)
+            workspace = _allocate_on(stream, lambda: torch.empty(n.value + 256, dtype=torch.uint8, device=codes.device))
         if scales.get_device() != self._index or (workspace.index if isinstance(workspace, KVWorkspace) else
                                                   workspace.get_device()) != self._index:
             raise ValueError("codes, scales and workspace must be on one device")
@@ -600,9 +611,10 @@ class KVCache:
     def empty(cls, n_pages: int, n_heads: int, head_dim: int, page_tokens: int = 64, code: str = "int8", device="cuda",
               workspace=None, stream=None):
         import torch
-        return cls(torch.empty((n_pages, n_heads, 2, page_tokens * head_dim), dtype=torch.uint8, device=device),
-                   torch.empty((n_pages, n_heads, page_tokens // KV_BLOCK, 2), dtype=torch.float32, device=device), code,
-                   workspace, stream)
+        codes, scales = _allocate_on(stream, lambda: (
+            torch.empty((n_pages, n_heads, 2, page_tokens * head_dim), dtype=torch.uint8, device=device),
+            torch.empty((n_pages, n_heads, page_tokens // KV_BLOCK, 2), dtype=torch.float32, device=device)))
+        return cls(codes, scales, code, workspace, stream)
 
     def _heads(self, h, x, n_heads, rows, what):
         """Checks per-head rows and describes them in h; returns the number of heads."""
@@ -617,8 +629,10 @@ class KVCache:
         h.data, h.token_stride, h.head_stride = x.data_ptr(), stride[0], stride[1]
         return shape[1]
 
-    def _out(self, x, shape, dtype, what):
+    def _out(self, x, shape, dtype, what, stream):
         if x is None:
+            if stream is not None:
+                return _allocate_on(stream, lambda: self._empty(shape, dtype=dtype, device=self._device))
             return self._empty(shape, dtype=dtype, device=self._device)
         if x.dtype is not dtype or tuple(x.shape) != shape or not x.is_contiguous() or x.get_device() != self._index:
             raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {shape} on the cache's device")
@@ -645,6 +659,7 @@ class KVCache:
         head strides that are multiples of 8); keys and the queries q are rotated by rope.
         Returns the rotated queries [total_q, heads, head_dim], or None without q."""
         rows, ks, vs, qs = batch.total_q, *self._args
+        on = self._on(stream)
         self._same_device(batch, "batch")
         self._heads(ks, k, self.n_heads, rows, "k")
         self._heads(vs, v, self.n_heads, rows, "v")
@@ -655,20 +670,21 @@ class KVCache:
             q_ref, nq, qo, q_ptr = None, 0, None, None
         else:
             q_ref, nq = self._arg_refs[2], self._heads(qs, q, None, rows, "q")
-            qo = self._out(q_out, (rows, nq, self.head_dim), self._bf16, "q_out")
+            qo = self._out(q_out, (rows, nq, self.head_dim), self._bf16, "q_out", stream)
             q_ptr = qo.data_ptr()
         st = self._lib.qlin_kv_append(self.ref, batch.ref, self._arg_refs[0], self._arg_refs[1], q_ref, nq, q_ptr, rope,
-                                      self.ws, self._on(stream))
+                                      self.ws, on)
         if st:
             raise QlinError(st, "qlin_kv_append")
         return qo
 
     def read(self, batch: KVBatch, stream=None):
         """The cached keys and values of the batch's tokens, bf16 [total_q, n_heads, head_dim] each."""
+        on = self._on(stream)
         self._same_device(batch, "batch")
         shape = (batch.total_q, self.n_heads, self.head_dim)
-        k, v = self._out(None, shape, self._bf16, "k"), self._out(None, shape, self._bf16, "v")
-        st = self._lib.qlin_kv_read(self.ref, batch.ref, k.data_ptr(), v.data_ptr(), self.ws, self._on(stream))
+        k, v = self._out(None, shape, self._bf16, "k", stream), self._out(None, shape, self._bf16, "v", stream)
+        st = self._lib.qlin_kv_read(self.ref, batch.ref, k.data_ptr(), v.data_ptr(), self.ws, on)
         if st:
             raise QlinError(st, "qlin_kv_read")
         return k, v
@@ -680,15 +696,16 @@ class KVCache:
         `sinks` ones.  scale defaults to head_dim ** -0.5.  Returns the output (and with
         return_lse the log-sum-exp of every row, fp32 [total_q, heads])."""
         rows = batch.total_q
+        on = self._on(stream)
         self._same_device(batch, "batch")
         nq = self._heads(self._args[2], q, None, rows, "q")
-        o = self._out(out, (rows, nq, self.head_dim), self._bf16, "out")
+        o = self._out(out, (rows, nq, self.head_dim), self._bf16, "out", stream)
         lse_ptr = None
         if lse is not None or return_lse:
-            lse = self._out(lse, (rows, nq), self._f32, "lse")
+            lse = self._out(lse, (rows, nq), self._f32, "lse", stream)
             lse_ptr = lse.data_ptr()
         st = self._lib.qlin_kv_attend(self.ref, batch.ref, self._arg_refs[2], nq, self._scale if scale is None else scale,
-                                      window, sinks, o.data_ptr(), lse_ptr, self.ws, self.ws_bytes, self._on(stream))
+                                      window, sinks, o.data_ptr(), lse_ptr, self.ws, self.ws_bytes, on)
         if st:
             raise QlinError(st, "qlin_kv_attend")
         return o if lse is None else (o, lse)

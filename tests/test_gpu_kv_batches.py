@@ -107,3 +107,30 @@ def test_errors_outlive_a_cache_on_the_same_workspace(qlin):
     assert second.poll_status() == qlin.QLIN_ERR_INVALID_ARG
     assert torch.equal(second.attend(su.batch, q), su.cache.attend(su.batch, q))
     su.ok()
+
+
+def pool_of(x):
+    """The stream whose pool a tensor's memory comes from."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= x.data_ptr() < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+
+
+def test_outputs_belong_to_the_stream_of_the_call(qlin):
+    """Memory of the current stream's pool may still be in use by kernels queued there, which the stream of
+    the call does not wait for: what a call on another stream makes comes from that stream's pool."""
+    s = torch.cuda.Stream()
+    su = Setup(qlin, "int8", 64, 16, 2, [3], [40])
+    k, v, q = bf(su.rows(2)), bf(su.rows(2)), bf(su.rows(4))
+    torch.cuda.synchronize()
+    for given in (s, s.cuda_stream):
+        qr = su.cache.append(su.batch, k, v, q=q, stream=given)
+        o, lse = su.cache.attend(su.batch, qr, return_lse=True, stream=given)
+        made = [qr, o, lse, *su.cache.read(su.batch, stream=given)]
+        cache = qlin.KVCache.empty(4, 2, 64, 16, stream=given)
+        made += [cache.codes, cache.scales, cache.workspace.memory]
+        s.synchronize()
+        assert [pool_of(x) for x in made] == [s.cuda_stream] * len(made)
+    here = su.cache.attend(su.batch, qr)
+    torch.cuda.synchronize()
+    assert pool_of(here) == torch.cuda.current_stream().cuda_stream and torch.equal(here, o)
