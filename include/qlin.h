@@ -361,7 +361,8 @@ qlin_status qlin_kv_read(const qlin_kv_cache* c, const qlin_kv_batch* b, void* K
  * query sees are not read, and their pages need no valid entry).  Query head h reads key/value
  * head h / (n_q_heads / n_heads).  With w_j = scale * q . k_j: O = sum e^(w_j) v_j / sum e^(w_j),
  * bf16 [total_q][n_q_heads][head_dim] contiguous; lse (optional) fp32 [total_q][n_q_heads] =
- * log sum e^(w_j).  A row that sees nothing gives O = 0, lse = -inf.  scale is positive and
+ * log sum e^(w_j).  A window or sinks over 2^30 are supported where they cover the whole page table.
+ * A row that sees nothing gives O = 0, lse = -inf.  scale is positive and
  * finite. */
 qlin_status qlin_kv_attend(const qlin_kv_cache* c, const qlin_kv_batch* b, const qlin_heads* Q, int n_q_heads,
                            float scale, int window, int sinks, void* O, float* lse, void* ws, size_t ws_bytes,

@@ -132,12 +132,17 @@ qlin_status qlin_kv_attend(const qlin_kv_cache* c, const qlin_kv_batch* b, const
   if (a.group == 0 || !(scale > 0.f) || !std::isfinite(scale) || window < 0 || sinks < 0) return QLIN_ERR_INVALID_ARG;
   if (ws_bytes < workspace_bytes(c->head_dim)) return QLIN_ERR_WORKSPACE;
   if (a.batch.n_seqs == 0 || a.batch.total_q == 0) return QLIN_OK;
+  // a window, or sinks, as long as the table hide nothing; shorter ones leave the kernels' differences of
+  // positions room in 32 bits up to 2^30
+  const int64_t positions = (int64_t)a.batch.pages_width * a.batch.page_tokens;
+  const bool hides = window > 0 && window < positions && sinks < positions;
+  if (hides && (window > 1 << 30 || sinks > 1 << 30)) return QLIN_ERR_UNSUPPORTED;
+  a.window = hides ? window : 0;
+  a.sinks = hides ? sinks : 0;
   if (!check_heads(Q, &a.q) || !O || !aligned(O, 16) || !aligned(lse, 4)) return QLIN_ERR_INVALID_ARG;
   a.o = (uint16_t*)O;
   a.lse = lse;
   a.scale = (float)((double)scale * 1.4426950408889634);
-  a.window = std::min(window, 1 << 30);  // positions are below 2^31: a wider window hides nothing
-  a.sinks = std::min(sinks, 1 << 30);
   a.counters = (uint32_t*)((uint8_t*)ws + kKvCountersOffset);
   a.partials = (float*)((uint8_t*)ws + kKvPartialsOffset);
   // Sequences with up to 16 query rows per key/value head go to the decoding kernel, the others

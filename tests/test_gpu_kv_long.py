@@ -274,3 +274,32 @@ def test_scores_far_out(qlin, qscale, q_lens, group):
         assert su.cache.poll_status() == 0
         _, _, vc, vs = su.held()
         assert bool(torch.isfinite(o).all()) and float(o.abs().max()) <= float((vc * vs).abs().max()) * 1.01
+
+
+@pytest.mark.parametrize("q_len", [1, 20])
+def test_positions_past_2_30(qlin, q_len):
+    """2^30 + 100 tokens in a table whose columns share two pages: a window over the whole table hides
+    nothing, the first tokens among it, one of which has nearly all the weight."""
+    D, page, T = 64, 1 << 20, (1 << 30) + 100
+    su = Long(qlin, "int8", D, page, 1, 2 * page, seed=q_len, keys=0.02)
+    x = torch.randn(D, generator=su.g, device="cuda")
+    k = torch.randn(2 * page, 1, D, generator=su.g, device="cuda") * 0.02
+    v = torch.randn(2 * page, 1, D, generator=su.g, device="cuda")
+    k[5, 0] = x * 40 / (D ** -0.5 * (x * x).sum())
+    su.store(k, v)
+    table = su.order[1].expand(1, -(-T // page)).clone()
+    table[0, 0] = su.order[0]
+    batch = qlin.KVBatch(i32([0, q_len]), i32([T]), table, q_len, q_len, T)
+    q = bf(x.expand(q_len, 1, D).contiguous())
+    want, lse = su.cache.attend(batch, q, return_lse=True)
+    _, _, vc, vs = su.held()
+    value = (vc[0, 5] * vs[0, 5]).float()
+    assert float((want.float() - value).abs().max()) < 0.02 and bool((lse > 38).all())
+    for window, sinks in ((2 ** 31 - 1, 0), (page * table.shape[1], 0), (100, 2 ** 31 - 1), (2 ** 30, 6)):
+        got, l = su.cache.attend(batch, q, window=window, sinks=sinks, return_lse=True)
+        if window != 2 ** 30:  # (that one hides some of the first tokens, not the sixth)
+            assert torch.equal(got, want) and torch.equal(l, lse)
+        assert float((got.float() - value).abs().max()) < 0.02
+    hidden, l = su.cache.attend(batch, q, window=2 ** 30, return_lse=True)
+    assert float(l.max()) < 30
+    assert su.cache.poll_status() == 0
