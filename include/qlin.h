@@ -345,7 +345,9 @@ qlin_status qlin_kv_init_workspace(void* ws, size_t bytes, qlin_stream stream);
  *           absmax over the finite new values, Q = 127 (int8) or 448 (e4m3)
  *   code  = round(x * (1/scale)), half to even, saturating; a NaN stores 0
  * and where the scale grew, the block's older codes become round(code * (old * (1/scale))).
- * A second append of the same tokens changes nothing. */
+ * A second append of the same tokens changes nothing.  Tokens are taken back by calling with a smaller
+ * kv_len (rejected drafts, say); a scale that they raised stays raised then, and the older codes of their
+ * block as coarse as it made them. */
 qlin_status qlin_kv_append(const qlin_kv_cache* c, const qlin_kv_batch* b, const qlin_heads* K, const qlin_heads* V,
                            const qlin_heads* Q, int n_q_heads, void* Q_out, const qlin_rope* rope, void* ws,
                            qlin_stream stream);

@@ -18,7 +18,8 @@
 // The arithmetic that decides a code is fp32, one rounding per operation (no fused
 // multiply-add), so codes and scales are reproducible bit for bit; the only division is one
 // reciprocal per block.  At prompt sizes the queries run at the memory's rate and the blocks at the
-// latency of their loads (16751 tokens of 32 + 2 x 8 heads of 128: 377 MB in 84 us, 4.5 TB/s); one
+// latency of their loads (16751 tokens of 32 + 2 x 8 heads of 128: 377 MB in 86 us, 4.4 TB/s; DRAM at 50%,
+// issue at 58%); one
 // token per sequence is launch and load latency (3 us for one, 7 us for 128 sequences).
 #include "kern_kv.cuh"
 

@@ -31,7 +31,10 @@
 // measured copy; 64 ragged ones (600 MB) 115 us, of which 3 us before the first keys, 85 at the
 // memory's rate and the rest the spread of the CTAs' ends and two joins of 3 us; one sequence of
 // 4100 tokens (8 MB) 13 us, all of it latency.  Six warps with two units of 16 KB in flight each fill
-// the shared memory; with 16 rows (NT = 2) five leave room for the larger partial results.
+// the shared memory; with 16 rows (NT = 2) five leave room for the larger partial results.  Heads of 64
+// are bound by the latency of those six warps instead: 64 sequences of 8192 tokens (537 MB) take 133 us,
+// 4.0 TB/s, with DRAM at 46%, issue at 29% and the tensor pipe at 9% in a capture: twice the softmax a
+// byte, and no unit full.
 #include "kern_kv.cuh"
 
 namespace qlin {

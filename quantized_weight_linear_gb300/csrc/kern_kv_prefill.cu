@@ -28,12 +28,12 @@
 // TMEM columns: scores of the two lanes (128 each), sums (D each).  Shared memory at D = 128:
 // queries 64 KB, five operand stages 160 KB.
 //
-// Bound by the shared memory and each lane's chain.  A tile of 128 keys and 256 rows takes 2048
-// tensor cycles; its MMAs read 192 KB of operands (1536 cycles of shared memory), the converters
-// write 64 KB more (512), and a lane's scores, softmax and product follow one another, 2350
-// cycles of them the softmax: 4500 cycles in all.  4096 queries over 32768 tokens, 32 heads, 8
-// key heads of 128 (2.06 TFLOP): 1.75 ms, 1175 TFLOP/s, 0.62 of the bf16 rate (ncu: tensor pipe
-// 45% active); the exponentials are not in the way (without them: 2% less).  Eight warps for the
+// Bound by each lane's chain.  A tile of 128 keys and 256 rows takes 2048 tensor cycles; its MMAs read
+// 192 KB of operands (1536 cycles of shared memory) and the converters write 64 KB more (512); but a
+// lane's scores, softmax (2350 cycles) and product follow one another, since the weights take the scores'
+// place: 4500 cycles in all, with no unit full.  4096 queries over 32768 tokens, 32 heads, 8 key heads of
+// 128 (2.06 TFLOP): 1.75 ms, 1175 TFLOP/s, 0.62 of the bf16 rate (ncu: tensor pipe 45% active, issue
+// 51%); the exponentials are not in the way (without them: 2% less).  Eight warps for the
 // conversion, two 64-key halves for the weights and one range of tiles a CTA are what measured
 // best against four warps, quarters, a tile of rows a CTA (ragged prompts 89 -> 77 us).
 #include <cstddef>
@@ -70,10 +70,10 @@ struct Seg {
   int part;                 // 0: the whole item, 1: its first piece, 2: another piece
 };
 
-// FEW: no sequence has over 128 rows a head.  Then the keys' bytes, not the tensor cores or the
-// softmax, bound the kernel: its registers go to the converters, who fetch two tiles ahead instead
-// of one, and the softmax warps read the scores in two halves (five drafts of 16 sequences: 97 ->
-// 78 us; the same split costs a prompt chunk 11%).
+// FEW: no sequence has over 128 rows a head.  Then the way of the keys' bytes into operands is the
+// longest part of the chain: the registers go to the converters, and the softmax warps read the
+// scores in two halves (five drafts of 16 sequences: 97 -> 78 us; the same split costs a prompt chunk
+// 11%).  Now 75 us, with no unit full: DRAM 31%, tensor pipe 25%, issue 38%, 40 of a tile's 128 rows used.
 template <int D, bool FEW>
 struct PreSmem {
   static constexpr int kOps = D == 128 ? 5 : 8;  // 16-bit operand stages
@@ -108,7 +108,9 @@ struct PreArgs {
   int row_blocks;  // upper bound of the row blocks of all sequences
 };
 
-// Registers: the launch gives every warp 96; the softmax warps hold a row's scores
+// Registers: the launch gives every warp 96; the softmax warps hold a row's scores.  (-Xptxas -v, spill
+// stores at head size 128: 128 bytes for int8, 148 for e4m3, 16 and 32 with FEW; at 64 up to 24.  Other
+// splits of the registers measured slower.)
 template <int N>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>

@@ -61,7 +61,11 @@ int launch_kv_append(int code, int head_dim, const KvView& c, const KvBatch& b, 
                      const KvHeads& q, int n_q_heads, uint16_t* q_out, const KvRope& r, void* stream);
 int launch_kv_read(int code, int head_dim, const KvView& c, const KvBatch& b, uint16_t* k_out, uint16_t* v_out,
                    void* stream);
-constexpr int kKvDecodeRows = 16;  // up to so many rows: kern_kv_decode.cu, more: kern_kv_prefill.cu
+// Up to so many rows: kern_kv_decode.cu (whose variants hold 8 and 16), more: kern_kv_prefill.cu.  us of
+// either, 8 key heads of 128, int8, at 4 / 8 / 16 rows: 64 sequences of 8192 177 / 180 / 259 against 335 /
+// 335 / 338; 16 of 4096 36 / 39 / 54 against 59 / 59 / 60; one of 4096 13.4 / 16.0 / 23.8 against 18.9 /
+// 19.0 / 19.3, the one case that it loses.
+constexpr int kKvDecodeRows = 16;
 // rows: most query rows per key/value head of a sequence
 int launch_kv_decode(int code, int head_dim, const KvAttendArgs& a, int rows, int sms, void* stream);
 constexpr int kKvPrefillRows = 256;  // rows of a row block of the latter
