@@ -422,8 +422,17 @@ class QLinear:
         qlin_set_workspace(self.handle, ws.data_ptr(), wb, max_M, stream)
         self.max_M = max_M
 
+    def _here(self, *tensors):
+        """The library launches on the current device: the layer and its tensors have to be there."""
+        import torch
+        device = torch._C._cuda_getDevice()
+        for x in (self.weights, *tensors):
+            if x is not None and x.get_device() != device:
+                raise ValueError(f"the current device is cuda:{device}, the layer or a tensor is on {x.device}")
+
     def __call__(self, X, out=None, stream=None):
         import torch
+        self._here(X, out)
         assert X.dtype == torch.bfloat16 and X.is_contiguous() and X.shape[-1] == self.K
         M = X.shape[0]
         Y = out if out is not None else torch.empty((M, self.N), dtype=torch.bfloat16, device=X.device)
@@ -431,11 +440,13 @@ class QLinear:
         return Y
 
     def forward_host(self, X_host, Y_host, X_dev, Y_dev, stream=None):
+        self._here(X_dev, Y_dev)
         qlin_forward_host(self.handle, X_host, Y_host, X_dev, Y_dev, X_host.shape[0], stream)
         return Y_host
 
     def act_quant(self, X, stream=None):
         import torch
+        self._here(X)
         M = X.shape[0]
         qx = torch.empty((M, self.K), dtype=torch.int8, device=X.device)
         sx = torch.empty((M,), dtype=torch.float32, device=X.device)
@@ -444,6 +455,7 @@ class QLinear:
 
     def forward_acc(self, X, stream=None):
         import torch
+        self._here(X)
         M = X.shape[0]
         acc = torch.empty((M, self.N), dtype=torch.int32, device=X.device)
         qlin_forward_acc(self.handle, X, acc, M, stream)
@@ -451,6 +463,7 @@ class QLinear:
 
     def dequant_device(self, stream=None):
         import torch
+        self._here()
         dt = torch.int8 if self.format == FMT_W8A8 else torch.float32
         out = torch.empty((self.N, self.K), dtype=dt, device=self.weights.device)
         qlin_dequant_device(self.handle, out, stream)
