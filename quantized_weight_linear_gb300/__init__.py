@@ -541,12 +541,14 @@ class KVBatch:
 
 
 def _allocate_on(stream, make):
-    """make() with its tensors belonging to `stream` (an int handle, a torch stream, or None: the current one):
-    memory that kernels queued elsewhere still use is not handed out to it."""
+    """make() with its tensors belonging to `stream` (as a call takes it; None: the current one): memory that
+    kernels queued elsewhere still use is not handed out to it."""
     import torch
     if stream is None:
         return make()
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream).value or 0)
+    with torch.cuda.stream(stream):
         return make()
 
 

@@ -1,5 +1,6 @@
 """The cache's Python binding without a GPU: what it refuses before the library is called.  Tensors are
 stand-ins that say they are on a device."""
+import contextlib
 import types
 
 import pytest
@@ -55,6 +56,9 @@ def world(qlin, monkeypatch):
     monkeypatch.setattr(qlin, "lib", lambda: w.lib)
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: w.device, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 0, raising=False)
+    w.allocated_on = []
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle: handle)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: w.allocated_on.append(s) or contextlib.nullcontext())
     monkeypatch.setattr(torch, "empty", lambda shape, dtype=None, device=None: Tensor(
         (shape,) if isinstance(shape, int) else tuple(shape), dtype, int(str(device).split(":")[1])))
 
@@ -98,6 +102,8 @@ def test_a_stream_of_another_device_is_refused(world):
     c, b, x = world.cache(0), world.batch(0), world.rows(0)
     here, there = (types.SimpleNamespace(device_index=d, cuda_stream=7) for d in (0, 1))
     c.attend(b, x, stream=here)
+    c.attend(b, x, stream=9)
+    assert world.allocated_on == [7, 9]  # their outputs belong to the stream of the call
     world.lib.calls[:] = []
     for call in (lambda: c.append(b, x, x, stream=there), lambda: c.attend(b, x, stream=there), lambda: c.read(b, stream=there),
                  lambda: c.poll_status(stream=there)):
